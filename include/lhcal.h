@@ -329,8 +329,9 @@ lhcal_status lhcal_matvec(lhcal_dtype xtype, const void* x, const float* x_scale
  * lhcal_matvec. Per row: r = x + residual rounded to dtype (r = x without a residual);
  * v = r * weight / sqrt(mean(r^2) + eps) in fp32; y = v rounded to dtype; per row (scale_block = 0)
  * or per 128 channels (LHCAL_SCALE_BLOCK, the last block may be shorter) y8_scale = max|v| / 448
- * in fp32 and y8 = E4M3 of v 448 / max|v| (a few fp32 roundings, then nearest even, at most 448; all
- * 0 where the scale is 0).
+ * in fp32 and y8 = E4M3 of v 448 / max|v| (nearest even, at most 448; all 0 where the scale is 0). The
+ * quotient leaves out the root, which is common to a row: with bf16 r and weight, r * weight is exact and y8 the
+ * E4M3 value nearest to the exact quotient; with fp32 ones two fp32 roundings come first.
  *   dtype    : LHCAL_F32 or LHCAL_BF16 of x, residual, residual_out and y.
  *   x        : [tokens, cin]; residual the same, or NULL; residual_out: out, r, or NULL (it must be
  *              NULL without a residual, and may be residual itself with the same stride).

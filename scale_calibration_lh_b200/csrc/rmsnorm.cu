@@ -142,21 +142,51 @@ __device__ __forceinline__ float weigh(const WT* weight, const Raw<T, K>& r, flo
   return m;
 }
 
-// A unit as E4M3 of v 448 / m (cvt.satfinite: at most 448; NaN stays NaN). The reciprocal is off by
-// an ulp, as a rounding more.
-template <int K>
+// Two fp32 values in a 64-bit register, as one instruction multiplies them.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// A unit as E4M3 of v 448 / m (cvt.satfinite: at most 448; NaN stays NaN). bf16 rows times bf16 weights have
+// 16 bits, so that 1 in 2400 of these quotients is a tie of two E4M3 values, which an error in the last place
+// would decide at random. Hence q0 = a / b by the approximate reciprocal, the exact remainder a - q0 b of one
+// fma, and q = q0 + (a - q0 b) / b, rounded once; a = 7/8 v and b = m / 512 are exact for 16 bits and do not
+// overflow. Against a product with 448 / m: 16384 x 4096 with residual 74.9 in place of 74.1 us, 16384 x 2560
+// without 36.9 in place of 35.5. For fp32 rows the pairs below cost more than they save (8192 x 4096: 77 us, 71
+// one by one).
+template <bool PAIRS, int K>
 __device__ __forceinline__ void quantise(uint8_t* to, const float* v, float m) {
-  const bool tiny = m < 1e-30f;  // 448 / m might overflow; 0 has no quotient
-  const float up = tiny ? 0x1p100f : 1.f;
+  const bool tiny = m < 0x1p-60f;  // 512 / m or the remainders might leave fp32's range; 0 has no quotient
+  const float b = m * (tiny ? 0x1p91f : 0x1p-9f), in = tiny ? 0.875f * 0x1p100f : 0.875f;
   float by;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(by) : "f"(m * up));
-  by = m > 0.f ? kE4m3Max * by : 0.f;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(by) : "f"(b));
+  by = m > 0.f ? by : 0.f;
   float q[K];
+  if constexpr (PAIRS) {
+    const uint64_t by2 = pair(by, by), minus_b2 = pair(-b, -b), in2 = pair(in, in);
 #pragma unroll
-  for (int i = 0; i < K; ++i) q[i] = v[i] * by;
-  if (tiny) {
+    for (int i = 0; i < K; i += 2) {
+      const uint64_t a = mul2(pair(v[i], v[i + 1]), in2), q0 = mul2(a, by2), left = fma2(q0, minus_b2, a);
+      asm("mov.b64 {%0, %1}, %2;" : "=f"(q[i]), "=f"(q[i + 1]) : "l"(fma2(left, by2, q0)));
+    }
+  } else {
 #pragma unroll
-    for (int i = 0; i < K; ++i) q[i] *= up;
+    for (int i = 0; i < K; ++i) {
+      const float a = v[i] * in, q0 = a * by;
+      q[i] = fmaf(fmaf(-q0, b, a), by, q0);
+    }
   }
   uint32_t h[K / 4];
 #pragma unroll
@@ -185,7 +215,7 @@ __device__ __forceinline__ void write(const Row<T>& row, bool by_block, int u, c
   const float s = m > 0.f ? m * rstd * (1.f / kE4m3Max) : 0.f;
   constexpr int kUnits = LHCAL_SCALE_BLOCK / K;
   if (by_block ? u % kUnits == 0 : u == 0) row.scale[by_block ? u / kUnits : 0] = s;
-  quantise<K>(row.y8 + u * K, v, s == 0.f ? 0.f : m);
+  quantise<sizeof(T) == 2, K>(row.y8 + u * K, v, s == 0.f ? 0.f : m);
 }
 
 // Maximum over the units of a 128-channel block, which lie in consecutive lanes of one warp.

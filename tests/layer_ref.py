@@ -128,3 +128,15 @@ def check_y8(y8, scale, v, scale_block, rel):
     half = torch.exp2(e - 4)  # half a step of 3 mantissa bits, or of the subnormals
     assert ((q - u).abs() <= half + u.abs() * (rel + 2.0 ** -22)).all()
     assert (q[se == 0] == 0).all()
+
+
+def e4m3_of_quotient(v, scale_block):
+    """E4M3 of 448 v / max|v| per row or 128 channels: nearest, ties to even, in fp64."""
+    n, cin = v.shape
+    blk = cin if scale_block == 0 else scale_block
+    nb = scale_blocks(cin, scale_block)
+    u = torch.nn.functional.pad(v, (0, nb * blk - cin)).view(n, nb, blk)
+    m = u.abs().amax(-1, keepdim=True)
+    u = torch.where(m > 0, 448.0 * u / m.clamp(min=1e-300), torch.zeros_like(u)).view(n, -1)[:, :cin]
+    step = torch.exp2(torch.floor(torch.log2(u.abs().clamp(min=2.0 ** -6))) - 3)
+    return torch.round(u / step) * step
