@@ -32,35 +32,12 @@
 // 114, 4 x 12288 x 4096 10.1 -> 9.5).
 #include "common.cuh"
 #include "matvec.cuh"
+#include "matvec_plan.cuh"
 
 namespace lhcal {
 namespace {
 
-constexpr int kMaxWarps = 20;               // that multiply; one more copies
-constexpr int kXBlock = LHCAL_SCALE_BLOCK;  // channels of one activation scale
-constexpr int kPieceK = 2 * kXBlock;        // channels of a warp
-constexpr int kTile = 16;                   // rows of a stage
-constexpr int kTokens = 8;                  // slots of an entry
-constexpr int kMaxSmem = 227 * 1024;
-constexpr int kStaticSmem = 512;            // what is kept for the barriers
-constexpr int kMinRows = 8;                 // rows a CTA takes at least
-constexpr int kMaxStages = 8;
-// Below as many tiles a CTA, one warp takes each: more would load the same activations (1 x 10 of 512
-// experts 1280 x 2560, 6 tiles: 11.0 against 12.6 us, 8 x 10, 44 tiles: 33.0 against 32.4).
-constexpr int kFewTiles = 16;
-
-struct Plan {
-  int wide;      // 16-byte reads of weights and whole words of scales; 8 bytes and single ones otherwise
-  int passes;
-  int wk, wr;    // warps over the channels and over the row tiles
-  int room;      // floats of a warp's sums
-  int stages;
-  int w_pitch, c_pitch;  // bytes of a row in a stage: weights, scale codes
-  int grid;
-  uint32_t per_row;  // 2^20 / slots of a row of x, rounded up: quotients of slots are exact
-  uint64_t per_cta;  // floor(2^64 / grid)
-  uint32_t stage, codes_at, red, list, smem;  // bytes: of a stage, its codes' place, and where the others begin
-};
+using Plan = MatvecPlan;
 
 template <int N>
 struct Int {
@@ -705,46 +682,8 @@ __global__ void __launch_bounds__(32 * WARPS, 1) matvec_kernel(const KernelArgs 
 }
 
 Plan make_plan(const MatvecArgs& m) {
-  Plan p = {};
-  const bool routed = m.experts != nullptr;
-  p.wide = m.cin % 64 == 0 && aligned(m.packed, 16) && aligned(m.codes, 4);
-  const int pieces = static_cast<int>(ceil_div(m.cin, kPieceK));
-  p.passes = static_cast<int>(ceil_div(pieces, kMaxWarps));
-  p.wk = static_cast<int>(ceil_div(pieces, p.passes));
-  p.wr = kMaxWarps / p.wk;
-  const int64_t entries = routed ? imin64(m.slots, m.groups) : ceil_div(m.slots, kTokens);
-  p.grid = static_cast<int>(imin64(kNumSms, ceil_div(m.rows * entries, kMinRows)));
-  p.per_row = (1u << 20) / static_cast<uint32_t>(m.per_row) + ((1u << 20) % static_cast<uint32_t>(m.per_row) != 0);
-  p.per_cta = p.grid == 1 ? 0 : ~uint64_t{0} / static_cast<uint64_t>(p.grid);
-  const int64_t all = ceil_div(ceil_div(m.rows * entries, p.grid) + 1, kTile);  // tiles of a CTA at most
-  if (all < kFewTiles) p.wr = 1;
-  if (p.passes == 1) {  // a tile's rows as they lie
-    p.w_pitch = static_cast<int>(m.cin / 2);
-    p.c_pitch = static_cast<int>(m.cin / kBlock);
-    p.codes_at = static_cast<uint32_t>(ceil_div(kTile * p.w_pitch + 16, 128) * 128);
-    p.stage = p.codes_at + static_cast<uint32_t>(ceil_div(kTile * p.c_pitch + 32, 128) * 128);
-  } else {
-    // Row by row, with the 16-byte units around it; 64 bytes apart modulo 128, so that the 8 lanes
-    // that read two rows together read 128 different bytes.
-    p.w_pitch = static_cast<int>(ceil_div(p.wk * kPieceK / 2 + 16, 128)) * 128 + 64;
-    p.c_pitch = p.wk * kPieceK / kBlock + 16;
-    p.codes_at = static_cast<uint32_t>(kTile * p.w_pitch);
-    p.stage = p.codes_at + static_cast<uint32_t>(kTile * p.c_pitch);
-  }
-  const uint32_t lists = routed ? (5u * (m.slots < 64 ? 64 : m.slots + 31 & ~31) + 1) * 4 : 0;
-  // Sums: a tile of 8 slots of a warp at least, all rows of a CTA at most, twice. What they leave
-  // of the memory goes to the stages.
-  const int64_t least = kTile * kTokens;
-  const int64_t fit = (kMaxSmem - kStaticSmem - static_cast<int64_t>(lists) - 3 * static_cast<int64_t>(p.stage)) / (2 * p.wk * 4) / least;
-  p.room = static_cast<int>(imax64(1, imin64(imin64(fit, 4), all)) * least);
-  const int64_t rest = kMaxSmem - kStaticSmem - static_cast<int64_t>(lists) - 2 * p.wk * p.room * 4;
-  p.stages = static_cast<int>(imin64(imin64(kMaxStages, rest / p.stage), imax64(2, all * p.passes)));
-  if (p.wr > p.stages) p.wr = p.stages;
-  p.red = static_cast<uint32_t>(p.stages) * p.stage;
-  p.list = p.red + 2u * p.wk * p.room * 4;
-  if (routed && p.list < (m.groups / 2u + 1) * 4) p.list = (m.groups / 2u + 1) * 4;  // the counts lie below it
-  p.smem = p.list + lists;
-  return p;
+  return make_matvec_plan({m.experts != nullptr, m.cin % 64 == 0 && aligned(m.packed, 16) && aligned(m.codes, 4), m.slots,
+                           m.per_row, m.groups, m.rows, m.cin, kNumSms});
 }
 
 template <bool WIDE, bool ROUTED, int WARPS>
