@@ -89,7 +89,10 @@ inline MatvecPlan make_matvec_plan(const MatvecSizes& m) {
   p.stages -= p.stages % p.wr;
   p.red = static_cast<uint32_t>(p.stages) * p.stage;
   p.list = p.red + 2u * p.wk * p.room * 4;
-  if (m.routed && p.list < (m.groups / 2u + 1) * 4) p.list = (m.groups / 2u + 1) * 4;  // the counts lie below it
+  // The counts of the experts, two a word, lie below the lists until those are made. The lists hold 8-byte pairs.
+  const uint32_t counts = (m.groups / 2u + 1) * 4;
+  if (m.routed && p.list < counts) p.list = counts;
+  p.list = (p.list + 15) & ~15u;
   p.smem = p.list + lists;
   return p;
 }

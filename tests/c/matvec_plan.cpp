@@ -35,6 +35,13 @@ void check(const MatvecSizes& m) {
   expect(last + 15 * p.w_pitch + k * (kPieceK / 2) + 3 * 16 + kXBlock / 2 + 16 + 8 <= p.smem, "weights read", m, p);
   expect(last + p.codes_at + 15 * p.c_pitch + k * (kPieceK / LHCAL_BLOCK) + 15 + 16 <= p.smem, "codes read", m, p);
   expect(p.red % 16 == 0, "sums", m, p);
+  // The slots' order, the entries, the experts, the counts' scan (8-byte pairs) and the work: `most` words each.
+  const uint32_t most = m.slots < 64 ? 64 : (m.slots + 31) & ~31u;
+  expect(!m.routed || p.list % 16 == 0, "list alignment", m, p);
+  expect(!m.routed || (p.list + 3 * most * 4) % 8 == 0, "scan alignment", m, p);
+  expect(!m.routed || p.list >= (m.groups / 2u + 1) * 4, "counts", m, p);
+  expect(!m.routed || p.list >= p.red + 2u * p.wk * p.room * 4, "sums below the lists", m, p);
+  expect(!m.routed || p.smem >= p.list + (5 * most + 1) * 4, "lists", m, p);
 }
 
 }  // namespace

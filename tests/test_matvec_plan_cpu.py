@@ -29,6 +29,7 @@ def report(program):
 
 @pytest.mark.parametrize("what", [
     "warps", "channels", "passes", "stages", "shared memory", "room", "stage alignment", "weights read", "codes read", "sums",
+    "list alignment", "scan alignment", "counts", "sums below the lists", "lists",
     "stage owners",  # a stage is always read by the same warps: a wait by parity needs a warp that saw the lap before
 ])
 def test_plan(report, what):
