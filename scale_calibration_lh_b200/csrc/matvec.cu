@@ -246,6 +246,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) matvec_kernel(const KernelArgs 
 
   const uint32_t entries = base + entries_at, order = base + order_at;
   const int warps = p.wk * p.wr;  // that multiply
+  const uint32_t failed_at = static_cast<uint32_t>(__cvta_generic_to_shared(&failed));
 
   const int my_k = warp % p.wk, my_r = warp / p.wk;
   auto channel_of = [&](int pass) { return (pass * p.wk + my_k) * kPieceK; };  // the warp's first in a pass
@@ -417,7 +418,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) matvec_kernel(const KernelArgs 
     // The CTA, and its shared memory, last until its copies are in, even if the others gave up.
     auto drain = [&]() {
       for (int s = lane; s < p.stages; s += 32)
-        for (int i = 0; i < kWaitLimit && !barrier_poll(bar + s * 16, s < stage ? phase : phase ^ 1); ++i) {}
+        for (int i = 0; i < kDrainLimit && !barrier_poll(bar + s * 16, s < stage ? phase : phase ^ 1); ++i) {}
     };
     for (; here.left > 0; here.advance(m, entries, p.room)) {
       for (int pass = 0; pass < p.passes; ++pass) {
@@ -428,7 +429,11 @@ __global__ void __launch_bounds__(32 * WARPS, 1) matvec_kernel(const KernelArgs 
         for (int r = 0; r < here.n; r += kTile, w += kTile * wstride, c += kTile * cstride) {
           const int n = min(kTile, here.n - r);
           const uint32_t full = bar + stage * 16, w_to = base + stage * p.stage, c_to = w_to + p.codes_at;
-          const bool free = lane != 0 || barrier_wait(full + 8, phase ^ 1, &failed);
+          bool free = lane != 0 || barrier_wait(full + 8, phase ^ 1, &failed);
+          // Warps free a stage whose wait ran out, too. What has not come in after kWaitLimit polls will not; but
+          // waits that give up at once leave copies in flight, which no other may follow. (In every build this
+          // would cost 1 x 467200 x 2560 121 us in place of 114.)
+          if (kImpatient && lane == 0) free = free && lds32(failed_at) == 0;
           if (!__all_sync(0xffffffffu, free)) return drain();
           if (lane != 0) {
           } else if (p.passes == 1) {
@@ -508,7 +513,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) matvec_kernel(const KernelArgs 
       }
       uint32_t off = 0;
       auto arrive = [&]() {
-        if (!barrier_wait(bar + at * 16, at_phase, &failed)) xs[0][0] = xs[0][1] = __int_as_float(0x7fffffff);
+        barrier_wait(bar + at * 16, at_phase, &failed);
         __syncwarp();
         off = at * p.stage;
       };
@@ -670,7 +675,9 @@ __global__ void __launch_bounds__(32 * WARPS, 1) matvec_kernel(const KernelArgs 
     for (int o = tid; o < here.n * pitch; o += 32 * warps) {
       const int n = o & (pitch - 1), r = o >> joined.shift;
       if (n >= joined.count) continue;
-      float v = 0.f;
+      // 0, or NaN from the block on in which a wait ran out: it set `failed` before its warp came to the barrier
+      // above, and a wait can pass for an earlier lap of its stage only after that.
+      float v = __uint_as_float(lds32(failed_at));
       for (int k = 0; k < p.wk; ++k) v += __uint_as_float(lds32(sums + (k * p.room + o) * 4));
       const int64_t y = (ROUTED ? static_cast<int>(lds32(order + 4 * (joined.first + n))) : joined.first + n) * m.ldy + here.row + r;
       if (m.ytype == LHCAL_F32)

@@ -79,7 +79,16 @@ __device__ __forceinline__ void wait_copies() {
 }
 
 // Barriers in shared memory that copies and products arrive at.
-constexpr int kWaitLimit = 1 << 20;  // polls of a barrier, after which the sums become NaN
+#ifdef LHCAL_IMPATIENT  // a build for tests, whose waits give up after one look
+#define LHCAL_POLL "mbarrier.test_wait"
+constexpr bool kImpatient = true;
+#else
+#define LHCAL_POLL "mbarrier.try_wait"
+constexpr bool kImpatient = false;
+#endif
+constexpr int kWaitLimit = kImpatient ? 0 : 1 << 20;  // polls of a barrier, after which the CTA's results become NaN
+constexpr int kDrainLimit = 1 << 20;  // the same of copies in flight, before a CTA that gave up ends
+constexpr int kNan = 0x7fffffff;      // fp32
 __device__ __forceinline__ void barrier_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
@@ -92,18 +101,18 @@ __device__ __forceinline__ void barrier_expect(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ bool barrier_poll(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      "{\n\t.reg .pred p;\n\t" LHCAL_POLL ".parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(done) : "r"(bar), "r"(parity) : "memory");
   return done != 0;
 }
-// False if the limit is reached, here or elsewhere in the CTA.
+// False if the limit is reached, here or elsewhere in the CTA: `failed` is then NaN's bits for good, else 0.
 __device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t parity, volatile int* failed) {
   if (barrier_poll(bar, parity)) return true;
   for (int i = 0; i < kWaitLimit; ++i) {
     if (barrier_poll(bar, parity)) return true;
     if (*failed) return false;
   }
-  *failed = 1;
+  *failed = kNan;
   return false;
 }
 // The largest magnitude of bf16 pairs so far, as two 16-bit numbers.
