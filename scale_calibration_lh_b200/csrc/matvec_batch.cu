@@ -116,6 +116,11 @@ __device__ __forceinline__ void product(uint32_t d, uint32_t a, uint64_t b, uint
       : "memory");
 }
 
+// The barrier is arrived at once the products that this thread has issued have ended.
+__device__ __forceinline__ void commit_products(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 // Into the same place of another CTA's shared memory.
 __device__ __forceinline__ void store_cluster(uint32_t at, int rank, float v) {
   asm volatile("{\n\t.reg .b32 there;\n\tmapa.shared::cluster.u32 there, %0, %1;\n\tst.shared::cluster.f32 [there], %2;\n\t}" ::"r"(at),
@@ -140,7 +145,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) matvec_batch_kernel(const Kern
   // The operand's layout: 128-byte swizzle, 8 rows every 1024 bytes.
   constexpr uint64_t kLayout = 2ull << 61 | 1ull << 46 | static_cast<uint64_t>(1024 / 16) << 32 | 1ull << 16;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t barriers[kGroups];
+  __shared__ __align__(8) uint64_t barriers[2 * kGroups];  // a warpgroup's: a product's end, the last ones' where a wait ran out
   __shared__ uint32_t tmem_at;
   __shared__ int failed;
   const MatvecArgs& m = ka.m;
@@ -154,6 +159,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) matvec_batch_kernel(const Kern
   const uint32_t raw = static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw)), base = (raw + 1023) & ~1023u;
   const uint32_t ring = base + p.ring + warp * (kSlots * kSlot);
   const uint32_t bar = static_cast<uint32_t>(__cvta_generic_to_shared(barriers + group));
+  const uint32_t failed_at = static_cast<uint32_t>(__cvta_generic_to_shared(&failed));
   const uint8_t* const codes_end = m.codes + m.rows * cstride;
 
   if (warp == 0) {
@@ -165,7 +171,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) matvec_batch_kernel(const Kern
   }
   if (tid == 0) {
     failed = 0;
-    for (int i = 0; i < kGroups; ++i) barrier_init(static_cast<uint32_t>(__cvta_generic_to_shared(barriers + i)), 1);
+    for (int i = 0; i < 2 * kGroups; ++i) barrier_init(static_cast<uint32_t>(__cvta_generic_to_shared(barriers + i)), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
 
@@ -293,7 +299,6 @@ __global__ void __launch_bounds__(32 * kWarps, 1) matvec_batch_kernel(const Kern
 
   for (int d = 0; d < kSlots - 1; ++d) copy_next();
   uint32_t at = ring, phase = 0, tmem = 0;  // the slot to use; the next product's parity; the warp's lanes of tensor memory
-  bool done = true;                         // every product ended
   for (int tile = cluster; tile < p.tiles; tile += p.clusters) {
     float acc[N];
 #pragma unroll
@@ -341,7 +346,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) matvec_batch_kernel(const Kern
 #pragma unroll
             for (int k = 0; k < kChunk / kStepK; ++k)
               product(sums, decoded + k * (kStepK / 2), kLayout | (from + k / 4 * kSlab + k % 4 * (kStepK * 2)) >> 4, kShape, k > 0);
-            asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+            commit_products(bar);
           }
           __syncwarp();
         };
@@ -367,7 +372,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) matvec_batch_kernel(const Kern
           }
         }
         if (pending >= 0) {
-          done &= barrier_wait(bar, phase ^ 1, &failed);
+          barrier_wait(bar, phase ^ 1, &failed);
           __syncwarp();
           tmem_fence_after();
 #pragma unroll
@@ -399,10 +404,6 @@ __global__ void __launch_bounds__(32 * kWarps, 1) matvec_batch_kernel(const Kern
         at = at + kSlot == ring + kSlots * kSlot ? ring : at + kSlot;
       }
     }
-    if (!done) {
-#pragma unroll
-      for (int n = 0; n < N; ++n) acc[n] = __int_as_float(0x7fffffff);
-    }
     // Join the warpgroups' sums through tensor memory: a warp adds up N / 4 tokens of its 32 rows.
     // Then the cluster's: the warps of the same place exchange tokens through the ring slot that each
     // read last, and each rank adds up some of the warp's tokens.
@@ -417,6 +418,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) matvec_batch_kernel(const Kern
       __syncthreads();
     tmem_fence_after();
     const float gs = __ldg(m.g);
+    const float lost = __uint_as_float(lds32(failed_at));  // 0, or NaN for good once a wait of the CTA ran out
     const int64_t row = static_cast<int64_t>(tile) * kTile + quarter * 32 + lane;
     uint8_t* const y_lane = static_cast<uint8_t*>(m.y) + (group * 4 * m.ldy + row) * p.y_bytes;
     auto put = [&](int j, float sum) {  // the warp's token j
@@ -437,7 +439,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) matvec_batch_kernel(const Kern
       tmem_load4x4(mine + n + group * 4, kColumns / kGroups, r);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        sum[i] = (__uint_as_float(r[i]) + __uint_as_float(r[4 + i])) + (__uint_as_float(r[8 + i]) + __uint_as_float(r[12 + i]));
+        sum[i] = ((__uint_as_float(r[i]) + __uint_as_float(r[4 + i])) + (__uint_as_float(r[8 + i]) + __uint_as_float(r[12 + i]))) + lost;
       if (p.split == 1) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) put(n / 4 + i, sum[i]);
@@ -469,6 +471,15 @@ __global__ void __launch_bounds__(32 * kWarps, 1) matvec_batch_kernel(const Kern
       __syncthreads();
     }
     tmem_fence_after();
+  }
+  // Products that no wait saw end still read the CTA's shared memory and write its tensor memory.
+  if (lds32(failed_at) != 0) {
+    if (quarter == 0 && lane == 0) {
+      commit_products(bar + 8 * kGroups);
+      for (int i = 0; i < kDrainLimit && !barrier_poll(bar + 8 * kGroups, 0); ++i) {}
+    }
+    __syncwarp();
+    __syncthreads();
   }
   if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_at), "n"(kColumns) : "memory");
