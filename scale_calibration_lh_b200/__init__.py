@@ -413,6 +413,12 @@ def _rows_of(t, name: str, rows: int, cols: int, dtype) -> int:
     return row if rows > 1 else cols
 
 
+def _address(t) -> int:
+    """The address of a tensor that is there. An empty one has none, and NULL would say that it is not: any
+    other number will do, since a call of no rows reads and writes nothing."""
+    return t.data_ptr() or 256
+
+
 def _n_scales(rows: int, cin: int, scale_block: int) -> int:
     return rows * (-(-cin // scale_block) if scale_block > 0 else 1)
 
@@ -447,7 +453,7 @@ def lhcal_matvec(x, packed, codes, g, y, experts=None, x_scale=None, scale_block
     slots = n
     if experts is not None:
         _need(experts, "experts", 0, i32)
-        slots, ep = experts.numel(), experts.data_ptr()
+        slots, ep = experts.numel(), _address(experts)
     ydt = y.dtype
     if ydt not in ids:
         raise TypeError(f"unsupported dtype {ydt}")

@@ -90,6 +90,23 @@ def test_matvec_without_tokens_checks_sizes_only(lib):
     assert _matvec(lib, **{**none, "cin": 8}) == L.ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("groups", [1, 3, 512])
+@pytest.mark.parametrize("n", [0, 2])
+def test_routed_call_without_slots_through_the_binding(lib, monkeypatch, groups, n):
+    """A step whose batch is empty: an empty tensor of experts has no address, and is not a missing one."""
+    monkeypatch.setattr(L, "_raw_stream", lambda stream: 0)
+    packed, codes = torch.zeros(groups, 8, 32, dtype=torch.uint8), torch.zeros(groups, 8, 4, dtype=torch.uint8)
+    x, y = torch.zeros(n, 64, dtype=torch.bfloat16), torch.zeros(0, 8)
+    e = torch.zeros(0, dtype=torch.int32)
+    L.lhcal_matvec(x, packed, codes, torch.ones(groups), y, experts=e)
+    q = torch.zeros(n, 64, dtype=E4M3)
+    L.lhcal_matvec(q, packed, codes, torch.ones(groups), y, experts=e.view(0, 1), x_scale=torch.ones(n, 1))
+    with pytest.raises(ValueError):
+        L.lhcal_matvec(x, packed, codes, torch.ones(groups), torch.zeros(1, 8), experts=e)
+    if n == 0 and groups == 1:
+        L.lhcal_matvec(x, packed, codes, torch.ones(1), y)
+
+
 def _norm(lib, **kw):
     a = dict(dtype=L.BF16, x=ctypes.c_void_p(1 << 20), tokens=4, cin=64, ldx=64, residual=None, ldr=64, residual_out=None,
              ldro=64, wtype=L.BF16, weight=None, eps=1e-6, y=ctypes.c_void_p(1 << 21), ldy=64, y8=None, ldy8=64,
