@@ -488,16 +488,16 @@ def lhcal_rmsnorm(x, weight=None, eps: float = 1e-6, residual=None, residual_out
             raise TypeError(f"unsupported dtype {weight.dtype}")
         wp, wtype = weight.data_ptr(), ids[weight.dtype]
     if residual is not None:
-        rp, ldr = residual.data_ptr(), _rows_of(residual, "residual", n, cin, dt)
+        rp, ldr = _address(residual), _rows_of(residual, "residual", n, cin, dt)
     if residual_out is not None:
-        rop, ldro = residual_out.data_ptr(), _rows_of(residual_out, "residual_out", n, cin, dt)
+        rop, ldro = _address(residual_out), _rows_of(residual_out, "residual_out", n, cin, dt)
     if y is not None:
-        yp, ldy = y.data_ptr(), _rows_of(y, "y", n, cin, dt)
+        yp, ldy = _address(y), _rows_of(y, "y", n, cin, dt)
     if y8 is not None:
-        y8p, ldy8 = y8.data_ptr(), _rows_of(y8, "y8", n, cin, e4m3)
+        y8p, ldy8 = _address(y8), _rows_of(y8, "y8", n, cin, e4m3)
     if y8_scale is not None:
         _need(y8_scale, "y8_scale", _n_scales(n, cin, scale_block), f32)
-        sp = y8_scale.data_ptr()
+        sp = _address(y8_scale)
     st = (_lib or load_library()).lhcal_rmsnorm(dtype, x.data_ptr(), n, cin, ldx, rp, ldr, rop, ldro, wtype, wp, eps, yp, ldy,
                                                 y8p, ldy8, sp, scale_block, _raw_stream(stream))
     if st:

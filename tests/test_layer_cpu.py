@@ -143,6 +143,21 @@ def test_rmsnorm_without_tokens(lib):
     assert _norm(lib, tokens=0, x=None) == L.OK
 
 
+@pytest.mark.parametrize("block", [0, 128])
+def test_rmsnorm_without_tokens_through_the_binding(lib, monkeypatch, block):
+    """Outputs of no rows have no address, and are not missing ones."""
+    monkeypatch.setattr(L, "_raw_stream", lambda stream: 0)
+    x = torch.zeros(0, 192, dtype=torch.bfloat16)
+    y8, s = torch.zeros(0, 192, dtype=E4M3), torch.zeros(0, R.scale_blocks(192, block))
+    L.lhcal_rmsnorm(x, y=torch.zeros_like(x))
+    L.lhcal_rmsnorm(x, torch.ones(192), residual=x, residual_out=torch.zeros_like(x), y=torch.zeros_like(x), y8=y8, y8_scale=s,
+                    scale_block=block)
+    L.lhcal_rmsnorm(x, y8=y8, y8_scale=s, scale_block=block)
+    for bad in (dict(), dict(y8=y8), dict(y=x, y8_scale=s), dict(y=x, residual_out=x)):
+        with pytest.raises(L.LhcalError):
+            L.lhcal_rmsnorm(x, **bad)
+
+
 def test_binding_rejects_what_the_library_would_misread(fake):
     packed, codes, g = torch.zeros(2, 8, 32, dtype=torch.uint8), torch.zeros(2, 8, 4, dtype=torch.uint8), torch.ones(2)
     x, y = torch.zeros(3, 64, dtype=torch.bfloat16), torch.zeros(6, 8)
