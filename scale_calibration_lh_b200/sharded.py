@@ -12,8 +12,9 @@ controls; "[2/3] Speed up layerwise GPTQ on MoE models", PR #2864: data-parallel
    scale of its shard; an all-reduce (MAX) gives the layer's. This is exact: g = fp32(amax /
    2688) is a monotone function of amax, so the maximum of the ranks' g is the g of the
    maximum amax;
-5. every rank sweeps its rows; with ``gather`` the codes and losses (and the fake-quantized
-   weights, when kept) are all-gathered so that every rank holds the whole layer's results.
+5. every rank sweeps its rows, and derives the bf16 fake-quantized weights and the 4-bit weights of
+   its codes when its buffers hold them; with ``gather`` the codes and losses (and the weights, when
+   kept) are all-gathered so that every rank holds the whole layer's results.
 
 For the activation-aware layer with the input quantizer fused, the quantizer's global scale is
 likewise the all-reduce (MAX) of the ranks' scales of their token shards, unless given.
@@ -62,8 +63,11 @@ def calibrate_sharded(mode, x_shard, w_shard, group=None, xq_shard=None, group_o
     group_offsets, token_ids : grouped layers, the routing of this rank's tokens (``shard_routing``).
     act_gx    : activation-aware with the fused input quantizer: the quantizer's global scale,
                 or None to take the all-reduce (MAX) of the ranks' scales of their shards.
-    Returns (buffers, results): the rank's Buffers (global H/P/counts/g, its rows' codes, wq and
-    loss) and, with ``gather``, a dict of the whole layer's codes and loss (and wq) in row order.
+    buffers   : this rank's Buffers, or None to make them; with want_wq16 or want_packed on every rank
+                or on none.
+    Returns (buffers, results): the rank's Buffers (global H/P/counts/g, its rows' codes, loss and
+    weights) and, with ``gather``, a dict of the whole layer's codes and loss (and wq, wq16 and packed
+    where the buffers hold them) in row order.
     """
     import torch
     import torch.distributed as dist
@@ -107,13 +111,17 @@ def calibrate_sharded(mode, x_shard, w_shard, group=None, xq_shard=None, group_o
     dist.all_reduce(b.g, op=dist.ReduceOp.MAX, group=group)
     # 5. this rank's rows
     ops.lhcal_scale_sweep(m, w_shard, b.h, b.g, b.codes, wq=b.wq, loss=b.loss, p=b.p)
+    if getattr(b, "wq16", None) is not None:
+        ops.lhcal_apply_scales(w_shard, b.g, b.codes, wq16=b.wq16)
+    if getattr(b, "packed", None) is not None:
+        ops.lhcal_pack_weights(w_shard, b.g, b.codes, b.packed)
     if not gather:
         return b, None
     return b, gather_rows(b, G, C, group=group)
 
 
 def gather_rows(buffers, groups: int, cin: int, group=None) -> dict:
-    """All-gather the ranks' row shards of codes and loss (and wq) into whole-layer tensors
+    """All-gather the ranks' row shards of codes and loss (and of the weights) into whole-layer tensors
     [G, R, ...] in row order (shards of different sizes are padded for the exchange)."""
     import torch
     import torch.distributed as dist
@@ -126,8 +134,8 @@ def gather_rows(buffers, groups: int, cin: int, group=None) -> dict:
     sizes = [int(s.item()) for s in sizes]
     rmax = max(sizes)
     out = {}
-    for name in ("codes", "loss", "wq"):
-        t = getattr(b, name)
+    for name in ("codes", "loss", "wq", "wq16", "packed"):
+        t = getattr(b, name, None)
         if t is None:
             continue
         pad = torch.zeros((t.shape[0], rmax) + tuple(t.shape[2:]), dtype=t.dtype, device=t.device)
