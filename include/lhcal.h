@@ -342,8 +342,9 @@ lhcal_status lhcal_matvec(lhcal_dtype xtype, const void* x, const float* x_scale
  *              (y8_scale 4). Outputs must not overlap inputs or each other, but for
  *              residual_out = residual.
  *   eps      : finite, >= 0.
- * Sums are fp32 in a fixed order: a mean(r^2) past fp32's range gives zeros, one of 0 with eps 0 no
- * finite y. tokens = 0 writes nothing. A row with NaN or infinity gives unspecified
+ * Sums are fp32 in a fixed order. A row whose squares or whose products with the weight would leave
+ * fp32's range is divided by a power of two first, which leaves v as it is: v is infinite only where it is
+ * past fp32's range itself, and NaN in a row of zeros with eps 0. tokens = 0 writes nothing. A row with NaN or infinity gives unspecified
  * values in that row and changes no other.
  */
 lhcal_status lhcal_rmsnorm(lhcal_dtype dtype, const void* x, int64_t tokens, int64_t cin, int64_t ldx,
