@@ -96,6 +96,35 @@ lhcal_status check_scale_block(int32_t scale_block) {
   return LHCAL_OK;
 }
 
+// Rows of a tensor in bytes; one row: dense.
+struct Rows {
+  const char* what;
+  const void* p;
+  int64_t rows, stride, width;
+  bool out;
+};
+
+// Whether a tensor's rows share a byte with [at, at + bytes).
+bool reaches(const Rows& a, const void* at, int64_t bytes) {
+  const int64_t d = static_cast<const char*>(at) - static_cast<const char*>(a.p);  // the first row that ends behind `at`
+  const int64_t i = a.rows == 1 || d < a.width ? 0 : (d - a.width) / a.stride + 1;
+  return i < a.rows && i * a.stride < d + bytes && i * a.stride + a.width > d;
+}
+
+// Whether two tensors share a byte. Row by row only where they reach over the same bytes and their strides differ.
+bool overlap(const Rows& a, const Rows& b) {
+  auto all = [](const Rows& t) { return Rows{"", t.p, 1, 0, (t.rows - 1) * t.stride + t.width, false}; };
+  if (!reaches(all(a), b.p, all(b).width)) return false;
+  if (a.rows > 1 && b.rows > 1 && a.stride == b.stride) {  // columns of one buffer: whether they are disjoint
+    const int64_t d = ((static_cast<const char*>(a.p) - static_cast<const char*>(b.p)) % a.stride + a.stride) % a.stride;
+    return d < b.width || d + a.width > a.stride;
+  }
+  const Rows &few = a.rows < b.rows ? a : b, &many = a.rows < b.rows ? b : a;
+  for (int64_t i = 0; i < few.rows; ++i)
+    if (reaches(many, static_cast<const char*>(few.p) + i * few.stride, few.width)) return true;
+  return false;
+}
+
 #define LHCAL_TRY(expr)                         \
   do {                                          \
     const lhcal_status st_ = (expr);            \
@@ -442,47 +471,34 @@ lhcal_status lhcal_rmsnorm(lhcal_dtype dtype, const void* x, int64_t tokens, int
   if ((y8 == nullptr) != (y8_scale == nullptr))
     return fail(LHCAL_ERR_INVALID_ARG, "y8 and y8_scale must both be set or both be NULL");
   if (y8 == nullptr && scale_block != 0) return fail(LHCAL_ERR_INVALID_ARG, "scale_block is only for y8");
-  const int64_t es = static_cast<int64_t>(elt_size(dtype));
-  struct Range {
-    const char* what;
-    const void* p;
-    int64_t ld, es;
-    bool out;
-  };
-  const Range r[] = {{"x", x, ldx, es, false},
-                     {"residual", residual, ldr, es, false},
-                     {"residual_out", residual_out, ldro, es, true},
-                     {"y", y, ldy, es, true},
-                     {"y8", y8, ldy8, 1, true}};
-  for (const Range& a : r) {
-    if (a.p == nullptr) continue;
-    if (a.ld < cin || (a.ld * a.es) % 16 != 0)
-      return fail(LHCAL_ERR_INVALID_ARG, "%s: row stride (%lld) must be >= cin (%lld) and a multiple of 16 bytes", a.what,
-                  (long long)a.ld, (long long)cin);
+  const int64_t es = static_cast<int64_t>(elt_size(dtype)), scales = scale_block ? ceil_div(cin, scale_block) : 1;
+  const Rows r[] = {{"x", x, tokens, ldx * es, cin * es, false},
+                    {"residual", residual, tokens, ldr * es, cin * es, false},
+                    {"residual_out", residual_out, tokens, ldro * es, cin * es, true},
+                    {"y", y, tokens, ldy * es, cin * es, true},
+                    {"y8", y8, tokens, ldy8, cin, true},
+                    {"y8_scale", y8_scale, 1, 0, tokens * scales * 4, true},
+                    {"weight", weight, 1, 0, cin * static_cast<int64_t>(elt_size(wtype)), false}};
+  for (int i = 0; i < 5; ++i) {
+    const int64_t e = i < 4 ? es : 1;
+    if (r[i].p != nullptr && (r[i].stride < r[i].width || r[i].stride % 16 != 0))
+      return fail(LHCAL_ERR_INVALID_ARG, "%s: row stride (%lld) must be >= cin (%lld) and a multiple of 16 bytes", r[i].what,
+                  (long long)(r[i].stride / e), (long long)cin);
   }
   if (tokens == 0) return LHCAL_OK;
-  LHCAL_TRY(check_device_ptr(x, 16, "x"));
-  for (const Range& a : r)
-    if (a.p != nullptr && a.p != x) LHCAL_TRY(check_device_ptr(a.p, 16, a.what));
-  if (weight != nullptr) LHCAL_TRY(check_device_ptr(weight, 16, "weight"));
-  if (y8_scale != nullptr) LHCAL_TRY(check_device_ptr(y8_scale, 4, "y8_scale"));
   // Rows are written while other rows are still to be read: an output may share no byte with
   // another tensor, but for the residual updated in place.
-  for (const Range& o : r) {
+  for (const Rows& o : r) {
     if (o.p == nullptr || !o.out) continue;
-    for (const Range& a : r) {
+    for (const Rows& a : r) {
       if (a.p == nullptr || &a == &o) continue;
-      if (o.p == residual_out && a.p == residual && o.p == a.p && o.ld == a.ld) continue;
-      const char *ob = static_cast<const char*>(o.p), *ab = static_cast<const char*>(a.p);
-      const int64_t ow = cin * o.es, aw = cin * a.es, ld = o.ld * o.es;
-      if (ld == a.ld * a.es) {  // disjoint column ranges of one buffer
-        const int64_t d = ((ob - ab) % ld + ld) % ld;
-        if (d >= aw && d + ow <= ld) continue;
-      }
-      if (ob < ab + (tokens - 1) * a.ld * a.es + aw && ab < ob + (tokens - 1) * ld + ow)
-        return fail(LHCAL_ERR_INVALID_ARG, "%s overlaps %s", o.what, a.what);
+      if (o.p == residual_out && a.p == residual && o.p == a.p && o.stride == a.stride) continue;
+      if (overlap(o, a)) return fail(LHCAL_ERR_INVALID_ARG, "%s overlaps %s", o.what, a.what);
     }
   }
+  LHCAL_TRY(check_device_ptr(x, 16, "x"));
+  for (const Rows& a : r)
+    if (a.p != nullptr && a.p != x) LHCAL_TRY(check_device_ptr(a.p, a.p == y8_scale ? 4 : 16, a.what));
   RmsnormArgs a = {};
   a.dtype = dtype; a.wtype = wtype;
   a.x = x; a.residual = residual; a.weight = weight;

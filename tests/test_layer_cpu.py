@@ -139,6 +139,38 @@ def test_rmsnorm_validates(lib, kw, status, word):
     assert _norm(lib, **kw) == status and word in _err(lib)
 
 
+X, Y = 1 << 20, 1 << 21  # of _norm: 4 rows of 64 channels
+
+
+@pytest.mark.parametrize("kw,word", [
+    (dict(weight=Y), "y overlaps weight"), (dict(weight=Y + 256), "y overlaps weight"),
+    (dict(weight=Y - 112), "y overlaps weight"),
+    (dict(weight=Y - 240, wtype=L.F32), "y overlaps weight"),
+    (dict(y8=1 << 22, y8_scale=(1 << 22) + 16), "y8 overlaps y8_scale"),
+    (dict(y8=1 << 22, y8_scale=Y + 508), "y overlaps y8_scale"),
+    (dict(y8=1 << 22, y8_scale=X), "y8_scale overlaps x"),
+    (dict(y8=1 << 22, y8_scale=Y - 16, scale_block=128, ldy=128, cin=128, ldx=128, ldy8=128), None),
+    (dict(y8=1 << 22, weight=1 << 23, y8_scale=(1 << 23) + 124), "y8_scale overlaps weight"),
+    (dict(y8=1 << 22, weight=1 << 23, y8_scale=(1 << 23) + 128), None),
+    (dict(residual=1 << 24, residual_out=1 << 25, weight=1 << 25), "residual_out overlaps weight"),
+    (dict(weight=X), None), (dict(weight=Y - 128), None), (dict(weight=Y + 512), None),  # inputs may share; next to y
+    (dict(weight=Y + 128, ldy=128), None),  # between two rows of y
+    (dict(weight=Y + 256 * 3 + 112, ldy=128), "y overlaps weight"), (dict(weight=Y + 256 * 3 + 128, ldy=128), None),
+    (dict(y8=Y + 128, y8_scale=1 << 22, ldy=128, ldy8=256), None),  # rows of y8 in every gap of y
+    (dict(y8=Y + 128, y8_scale=1 << 22, ldy=128, ldy8=512), None),  # in every second one
+    (dict(y8=Y + 128, y8_scale=1 << 22, ldy=128, ldy8=144), "overlaps"),
+    (dict(ldx=0), "stride"), (dict(ldy=-64), "stride"),
+    (dict(residual=Y + 128, residual_out=Y + 128, ldr=128, ldro=128, ldy=128), None),  # columns of one buffer
+    (dict(residual=Y + 112, residual_out=Y + 112, ldr=128, ldro=128, ldy=128), "overlaps"),
+])
+def test_rmsnorm_refuses_overlaps_of_all_its_tensors(lib, monkeypatch, kw, word):
+    """Outputs against the weight and the scales, too. None: no overlap, so that the call goes on to the
+    pointers, which are no device memory here."""
+    kw = {k: ctypes.c_void_p(v) if k in ("weight", "y8", "y8_scale", "residual", "residual_out") else v for k, v in kw.items()}
+    assert _norm(lib, **kw) == L.ERR_INVALID_ARG
+    assert (word or "device memory") in _err(lib) or (word is None and "query pointer" in _err(lib)), _err(lib)
+
+
 def test_rmsnorm_without_tokens(lib):
     assert _norm(lib, tokens=0, x=None) == L.OK
 
