@@ -312,7 +312,8 @@ lhcal_status lhcal_unpack_weights(const uint8_t* packed, const uint8_t* codes, c
  *             their scale codes [groups, rows, cin/16] (E4M3 bit patterns in [0, 126], as every
  *             call here writes them; others give unspecified results) and global scales [groups].
  *   ytype, y: LHCAL_BF16 (rounded once from fp32) or LHCAL_F32 [slots, rows], row stride ldy
- *             elements (>= rows), aligned to its element size; not overlapping an input.
+ *             elements (>= rows), aligned to its element size; overlapping no input
+ *             (LHCAL_ERR_INVALID_ARG).
  * The weights' values q * v are exact in the products; sums are fp32 in an order fixed by the
  * sizes and the routing, so that results are the same call after call. Activations
  * below 2^-29 of the largest magnitude of their 128 channels can lose bits of their own. NaN and

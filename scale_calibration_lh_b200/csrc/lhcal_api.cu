@@ -35,9 +35,17 @@ lhcal_status fail(lhcal_status st, const char* fmt, ...) {
   return st;
 }
 
-lhcal_status check_device_ptr(const void* p, size_t align, const char* what) {
+namespace {
+lhcal_status check_ptr(const void* p, size_t align, const char* what) {
   if (p == nullptr) return fail(LHCAL_ERR_INVALID_ARG, "%s is NULL", what);
   if (!aligned(p, align)) return fail(LHCAL_ERR_INVALID_ARG, "%s is not %zu-byte aligned", what, align);
+  return LHCAL_OK;
+}
+}  // namespace
+
+lhcal_status check_device_ptr(const void* p, size_t align, const char* what) {
+  const lhcal_status st = check_ptr(p, align, what);
+  if (st != LHCAL_OK) return st;
   cudaPointerAttributes attr;
   cudaError_t e = cudaPointerGetAttributes(&attr, p);
   if (e != cudaSuccess) {
@@ -436,6 +444,18 @@ lhcal_status lhcal_matvec(lhcal_dtype xtype, const void* x, const float* x_scale
                 (long long)ldy, (long long)cin, (long long)rows);
   if ((ldx * es) % 16 != 0) return fail(LHCAL_ERR_INVALID_ARG, "ldx * element size must be a multiple of 16 bytes");
   if (slots == 0) return LHCAL_OK;
+  // CTAs write their rows of y while others still read.
+  const int64_t weights = groups * rows * cin, scales = scale_block ? ceil_div(cin, scale_block) : 1;
+  const Rows out = {"y", y, slots, ldy * static_cast<int64_t>(elt_size(ytype)), rows * static_cast<int64_t>(elt_size(ytype)), true};
+  const Rows in[] = {{"x", x, x_rows, ldx * es, cin * es, false},
+                     {"x_scale", x_scale, 1, 0, x_rows * scales * 4, false},
+                     {"experts", experts, 1, 0, slots * int64_t{4}, false},
+                     {"packed", packed, 1, 0, weights / 2, false},
+                     {"codes", codes, 1, 0, weights / LHCAL_BLOCK, false},
+                     {"g", g, 1, 0, groups * int64_t{4}, false}};
+  LHCAL_TRY(check_ptr(x, 16, "x"));
+  for (const Rows& a : in)
+    if (y != nullptr && a.p != nullptr && overlap(out, a)) return fail(LHCAL_ERR_INVALID_ARG, "y overlaps %s", a.what);
   LHCAL_TRY(check_device_ptr(x, 16, "x"));
   if (xtype == LHCAL_E4M3) LHCAL_TRY(check_device_ptr(x_scale, 4, "x_scale"));
   if (experts != nullptr) LHCAL_TRY(check_device_ptr(experts, 4, "experts"));

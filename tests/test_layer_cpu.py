@@ -83,6 +83,28 @@ def test_matvec_validates(lib, kw, status, word):
     assert _matvec(lib, **kw) == status and word in _err(lib)
 
 
+Y0 = 1 << 20  # of the calls below: fp32 y [2, 8], 64 bytes in all
+
+
+@pytest.mark.parametrize("kw,word", [
+    (dict(x=Y0), "y overlaps x"), (dict(x=Y0 - 240), "y overlaps x"), (dict(x=Y0 - 256), None), (dict(x=Y0 + 64), None),
+    (dict(packed=Y0 + 56), "y overlaps packed"), (dict(packed=Y0 - 248), "y overlaps packed"), (dict(packed=Y0 - 256), None),
+    (dict(codes=Y0 - 31), "y overlaps codes"), (dict(codes=Y0 - 32), None), (dict(g=Y0 + 60), "y overlaps g"),
+    (dict(g=Y0 - 4), None), (dict(experts=Y0 - 8), None), (dict(experts=Y0 - 4), "y overlaps experts"),
+    (dict(xtype=L.E4M3, x_scale=Y0 - 4), "y overlaps x_scale"), (dict(xtype=L.E4M3, x_scale=Y0 - 8), None),
+    (dict(x=Y0 + 32, ldx=80, ldy=40), None),  # x and y as columns of one buffer
+    (dict(x=Y0 + 16, ldx=80, ldy=40), "y overlaps x"),
+])
+def test_matvec_refuses_overlaps(lib, kw, word):
+    """A CTA reads its inputs while another writes y. None: no overlap, so that the call goes on to the
+    pointers, which are no device memory here."""
+    at = dict(x=1 << 24, packed=1 << 25, codes=1 << 26, g=1 << 27, y=Y0)
+    at.update(kw)
+    assert _matvec(lib, **{k: ctypes.c_void_p(v) if k in ("x", "x_scale", "packed", "codes", "g", "experts", "y") else v
+                           for k, v in at.items()}) == L.ERR_INVALID_ARG
+    assert (word or "device memory") in _err(lib) or (word is None and "query pointer" in _err(lib)), _err(lib)
+
+
 def test_matvec_without_tokens_checks_sizes_only(lib):
     none = dict(x_rows=0, slots=0, x=None, y=None, packed=None, codes=None, g=None)
     assert _matvec(lib, **none) == L.OK
