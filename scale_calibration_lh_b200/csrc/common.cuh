@@ -130,7 +130,7 @@ struct MatvecArgs {
 };
 
 lhcal_status launch_matvec(const MatvecArgs& a, cudaStream_t stream);
-// One layer, with a batch of tokens or many channels (launch_matvec goes on to it).
+// One layer, with a batch of tokens, or many channels and not many rows (launch_matvec goes on to it).
 lhcal_status launch_matvec_batch(const MatvecArgs& a, cudaStream_t stream);
 
 // Arguments of lhcal_rmsnorm, checked.

@@ -1,4 +1,4 @@
-// Products of a few tokens with packed NVFP4 weights, of one layer or of routed experts.
+// Products of up to 8 tokens with one layer's packed NVFP4 weights, or of routed slots with their experts'.
 //
 // y_{i,r} = g_e * sum_c (q_{e,r,c} v_{e,r,c/16}) x_{i,c}, with e the slot's expert.
 //
@@ -197,9 +197,8 @@ __device__ __forceinline__ Entry read_entry(const MatvecArgs& m, uint32_t entrie
     e.first = v >> 16 & 0xfff;
     e.count = v >> 28;
   } else {
-    e.expert = 0;
-    e.first = k * kTokens;
-    e.count = min(m.slots - e.first, kTokens);
+    e.expert = e.first = 0;
+    e.count = min(m.slots, kTokens);  // as it is; without the bound 1 x 467200 x 2560 takes 135 us in place of 114
   }
   e.shift = e.count <= 2 ? 1 : e.count <= 4 ? 2 : 3;
   return e;
@@ -308,7 +307,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) matvec_kernel(const KernelArgs 
     }
   };
 
-  int n_entries = (m.slots + kTokens - 1) / kTokens;
+  int n_entries = 1;  // one layer
   int held = -1;  // whose activations x holds
   if (tid == 0) {
     failed = 0;
@@ -380,12 +379,10 @@ __global__ void __launch_bounds__(32 * WARPS, 1) matvec_kernel(const KernelArgs 
     here.left = share[2];
     last = share[3];
   } else {
-    const uint64_t total = static_cast<uint64_t>(n_entries) * rows;
-    const uint64_t begin = cut(total, blockIdx.x), end = cut(total, blockIdx.x + 1);
-    here.entry = n_entries > 1 ? static_cast<int>(begin / rows) : 0;
-    here.row = static_cast<int>(begin - static_cast<uint64_t>(here.entry) * rows);
+    const uint64_t begin = cut(rows, blockIdx.x), end = cut(rows, blockIdx.x + 1);
+    here.entry = last = 0;
+    here.row = static_cast<int>(begin);
     here.left = static_cast<int>(end - begin);
-    last = 0;
   }
   if (here.left <= 0) return;
   here.clip(m, entries, p.room);
@@ -720,11 +717,16 @@ lhcal_status launch_warps(const KernelArgs& ka, cudaStream_t stream) {
 }  // namespace
 
 lhcal_status launch_matvec(const MatvecArgs& m, cudaStream_t stream) {
-  // One layer with more than 8 tokens, or more channels than the warps hold at once: decoding each weight
-  // once for all tokens wins there (16 x 4096 x 4096: 8.4 against 13.4 us, 64: 16.5 against 31, 17 x 4096 x
-  // 12288: 17.5 against 35). Fewer tokens would fill half of its columns (8 x 4096 x 4096: 8.2 against 7.2 us).
-  if (m.experts == nullptr && (m.slots > kTokens || m.cin > kMaxWarps * kPieceK))
-    return launch_matvec_batch(m, stream);
+  // One layer with more than 8 tokens: decoding each weight once for all of them wins (16 x 4096 x 4096: 8.4
+  // against 13.4 us, 64: 16.5 against 31, 17 x 4096 x 12288: 17.5 against 35). Fewer tokens would fill half of its
+  // columns (8 x 4096 x 4096: 8.2 against 7.2 us), but where the warps do not hold all channels at once, the
+  // kernel here comes back to each block of rows with other activations, and its clusters split the channels
+  // instead: better for small layers (1 x 4096 x 12288 12.4 against 14.0, 8 14.5 against 15.1, 1 x 1280 x 40960 18.9
+  // against 24.2), not for large ones, which are several waves of clusters (1 x 8192 x 8192 19.2 against 16.9, 1 x
+  // 16384 x 12288 46.7 against 38.6, 8 48.4 against 43.0). 56 Mi weights part most of the sizes measured (a few lie up
+  // to 9% on the wrong side: 8 x 24576 x 6144 38.0 against 41.1, 1 x 2560 x 20480 20.0 against 18.3).
+  const bool passes = m.cin > kMaxWarps * kPieceK;
+  if (m.experts == nullptr && (m.slots > kTokens || (passes && m.rows * m.cin < int64_t{56} << 20))) return launch_matvec_batch(m, stream);
   const KernelArgs ka = {m, make_plan(m)};
   const bool routed = m.experts != nullptr;
   if (ka.p.wide) return routed ? launch_warps<true, true>(ka, stream) : launch_warps<true, false>(ka, stream);

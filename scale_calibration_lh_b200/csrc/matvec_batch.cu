@@ -1,5 +1,5 @@
-// Products of a batch of tokens (up to 64) with one layer's packed NVFP4 weights, or of few tokens with
-// many channels: y_{i,r} = g * sum_c (q_{r,c} v_{r,c/16}) x_{i,c}.
+// Products of a batch of tokens (up to 64) with one layer's packed NVFP4 weights, or of few tokens
+// with many channels and not many rows: y_{i,r} = g * sum_c (q_{r,c} v_{r,c/16}) x_{i,c}.
 //
 // Decoding is what costs here, so each weight is decoded once for all tokens: to fp16 (q v is exact),
 // a row a lane, into tensor memory, where tcgen05.mma takes its 128 x 128 operand from. The

@@ -52,7 +52,7 @@ inline MatvecPlan make_matvec_plan(const MatvecSizes& m) {
   p.passes = static_cast<int>(ceil(pieces, kMaxWarps));
   p.wk = static_cast<int>(ceil(pieces, p.passes));
   p.wr = static_cast<int>(least_of(kMaxWarps / p.wk, kStages));
-  const int64_t entries = m.routed ? least_of(m.slots, m.groups) : ceil(m.slots, kTokens);
+  const int64_t entries = m.routed ? least_of(m.slots, m.groups) : 1;
   p.grid = static_cast<int>(least_of(m.sms, ceil(m.rows * entries, kMinRows)));
   p.per_row = (1u << 20) / static_cast<uint32_t>(m.per_row) + ((1u << 20) % static_cast<uint32_t>(m.per_row) != 0);
   p.per_cta = p.grid == 1 ? 0 : ~uint64_t{0} / static_cast<uint64_t>(p.grid);
