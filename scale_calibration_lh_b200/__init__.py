@@ -419,8 +419,12 @@ def _address(t) -> int:
     return t.data_ptr() or 256
 
 
-def _n_scales(rows: int, cin: int, scale_block: int) -> int:
-    return rows * (-(-cin // scale_block) if scale_block > 0 else 1)
+def _need_scales(t, name: str, rows: int, cin: int, scale_block: int):
+    """fp32 scales of [rows, cin] values: at least as many, and with rows of the call's number of scales."""
+    each = -(-cin // scale_block) if scale_block > 0 else 1
+    _need(t, name, rows * each, _types()[1])
+    if rows and t.dim() > 1 and t.shape[-1] != each and (each > 1 or t.shape[0] == rows):
+        raise ValueError(f"{name} is {tuple(t.shape)}; scale_block {scale_block} has {each} for each of {rows} rows")
 
 
 def lhcal_matvec(x, packed, codes, g, y, experts=None, x_scale=None, scale_block: int = 0, stream=None):
@@ -448,7 +452,7 @@ def lhcal_matvec(x, packed, codes, g, y, experts=None, x_scale=None, scale_block
     ldx = _rows_of(x, "x", n, cin, xdt)
     xsp = ep = None
     if x_scale is not None:
-        _need(x_scale, "x_scale", _n_scales(n, cin, scale_block), f32)
+        _need_scales(x_scale, "x_scale", n, cin, scale_block)
         xsp = x_scale.data_ptr()
     slots = n
     if experts is not None:
@@ -470,7 +474,7 @@ def lhcal_rmsnorm(x, weight=None, eps: float = 1e-6, residual=None, residual_out
     """RMS norm of x + residual [tokens, C] (fp32 or bf16), into y (x's type) and / or float8_e4m3fn
     y8 with fp32 y8_scale [tokens, 1] (scale_block 0) or [tokens, ceil(C/128)] (128); residual_out
     receives x + residual and may be residual itself."""
-    _, f32, e4m3, _, _, ids = _types()
+    _, _, e4m3, _, _, ids = _types()
     shape = x.shape
     if len(shape) != 2:
         raise ValueError(f"x must be [tokens, cin], got {tuple(shape)}")
@@ -496,7 +500,7 @@ def lhcal_rmsnorm(x, weight=None, eps: float = 1e-6, residual=None, residual_out
     if y8 is not None:
         y8p, ldy8 = _address(y8), _rows_of(y8, "y8", n, cin, e4m3)
     if y8_scale is not None:
-        _need(y8_scale, "y8_scale", _n_scales(n, cin, scale_block), f32)
+        _need_scales(y8_scale, "y8_scale", n, cin, scale_block)
         sp = _address(y8_scale)
     st = (_lib or load_library()).lhcal_rmsnorm(dtype, x.data_ptr(), n, cin, ldx, rp, ldr, rop, ldro, wtype, wp, eps, yp, ldy,
                                                 y8p, ldy8, sp, scale_block, _raw_stream(stream))

@@ -246,6 +246,23 @@ def test_binding_rejects_what_the_library_would_misread(fake):
         L.lhcal_unpack_weights(packed, codes, g, wq=torch.zeros(1, 8, 64))
 
 
+def test_scales_of_another_block_are_rejected(fake):
+    """[n, C / 128] scales with the default of one a row (or the reverse) would be read as other rows' scales."""
+    packed, codes, g = torch.zeros(1, 8, 128, dtype=torch.uint8), torch.zeros(1, 8, 16, dtype=torch.uint8), torch.ones(1)
+    q, n = torch.zeros(3, 256, dtype=E4M3), torch.zeros(3, 256, dtype=torch.bfloat16)
+    for cols, block in ((2, 0), (3, 128), (1, 128)):
+        s = torch.ones(3, cols)
+        with pytest.raises(ValueError):
+            L.lhcal_matvec(q, packed, codes, g, torch.zeros(3, 8), x_scale=s, scale_block=block)
+        with pytest.raises(ValueError):
+            L.lhcal_rmsnorm(n, y8=q, y8_scale=s, scale_block=block)
+    assert not fake.names()
+    for s, block in ((torch.ones(3, 1), 0), (torch.ones(3), 0), (torch.ones(64, 1), 0), (torch.ones(3, 2), 128),
+                     (torch.ones(64, 2), 128), (torch.ones(6), 128), (torch.ones(1, 3), 0)):
+        L.lhcal_matvec(q, packed, codes, g, torch.zeros(3, 8), x_scale=s, scale_block=block)
+        L.lhcal_rmsnorm(n, y8=q, y8_scale=s, scale_block=block)
+
+
 def test_one_row_passes_no_stride(fake):
     """A single row of a wider (or oddly strided) buffer is dense whatever its stride says."""
     packed, codes, g = torch.zeros(1, 8, 32, dtype=torch.uint8), torch.zeros(1, 8, 4, dtype=torch.uint8), torch.ones(1)
