@@ -526,7 +526,7 @@ class Buffers:
         self.h = None if self.mode == MSE else torch.empty(hshape, dtype=torch.float32, device=device)
         self.p = torch.empty(hshape, dtype=torch.float32, device=device) if self.mode == ACT_AWARE else None
         self.counts = torch.empty(groups, dtype=torch.int64, device=device)
-        self.g = torch.empty(groups, dtype=torch.float32, device=device)
+        self.g = torch.zeros(groups, dtype=torch.float32, device=device)
         self.codes = torch.empty((groups, rows, nblk), dtype=torch.uint8, device=device)
         self.wq = torch.empty((groups, rows, cin), dtype=torch.float32, device=device) if want_wq else None
         self.loss = torch.empty((groups, rows, nblk), dtype=torch.float32, device=device) if want_loss else None

@@ -308,3 +308,16 @@ def test_reference_decodes_the_formats():
     assert R.e4m3_table()[:127].tolist() == torch.arange(127, dtype=torch.uint8).view(E4M3).float().tolist()
     packed = torch.tensor([[0x10, 0xF2] + [0] * 6], dtype=torch.uint8)
     assert R.weight_values(packed, torch.tensor([[57]], dtype=torch.uint8))[0, :4].tolist() == [0.0, 0.5625, 1.125, -6.75]
+
+
+def test_buffers_scales_begin_defined(monkeypatch, fake):
+    """Global scales that no call has written yet compare equal to a copy of them, whatever lay in memory before."""
+    empty = torch.empty
+
+    def dirty(*a, **k):
+        t = empty(*a, **k)
+        return t.fill_(float("nan")) if t.is_floating_point() else t
+
+    monkeypatch.setattr(torch, "empty", dirty)
+    b = L.Buffers("mse", 0, 64, 8, 2, L.BF16, "cpu")
+    assert torch.equal(b.g, b.g.clone())
