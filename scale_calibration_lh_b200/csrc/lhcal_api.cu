@@ -445,7 +445,7 @@ lhcal_status lhcal_matvec(lhcal_dtype xtype, const void* x, const float* x_scale
   if ((ldx * es) % 16 != 0) return fail(LHCAL_ERR_INVALID_ARG, "ldx * element size must be a multiple of 16 bytes");
   if (slots == 0) return LHCAL_OK;
   // CTAs write their rows of y while others still read.
-  const int64_t weights = groups * rows * cin, scales = scale_block ? ceil_div(cin, scale_block) : 1;
+  const int64_t weights = imin64(rows * cin, (int64_t{1} << 56) / groups) * groups, scales = scale_block ? ceil_div(cin, scale_block) : 1;
   const Rows out = {"y", y, slots, ldy * static_cast<int64_t>(elt_size(ytype)), rows * static_cast<int64_t>(elt_size(ytype)), true};
   const Rows in[] = {{"x", x, x_rows, ldx * es, cin * es, false},
                      {"x_scale", x_scale, 1, 0, x_rows * scales * 4, false},

@@ -267,6 +267,7 @@ __device__ __noinline__ void scaled_row(const RmsnormArgs a, int64_t at, float2*
     if (span > 32) __syncthreads();  // the last sums are read
     block_reduce(sum, top, red);
   };
+  __syncwarp();  // other threads have written residual_out: of one warp here, else block_reduce's barrier lies between
   float v[K], sum = 0.f, top = 0.f;
   for (int u = tid; u < units; u += span) {
     get_r(u, v);

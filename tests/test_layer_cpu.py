@@ -92,6 +92,7 @@ Y0 = 1 << 20  # of the calls below: fp32 y [2, 8], 64 bytes in all
     (dict(codes=Y0 - 31), "y overlaps codes"), (dict(codes=Y0 - 32), None), (dict(g=Y0 + 60), "y overlaps g"),
     (dict(g=Y0 - 4), None), (dict(experts=Y0 - 8), None), (dict(experts=Y0 - 4), "y overlaps experts"),
     (dict(xtype=L.E4M3, x_scale=Y0 - 4), "y overlaps x_scale"), (dict(xtype=L.E4M3, x_scale=Y0 - 8), None),
+    (dict(experts=1 << 28, groups=65535, rows=2 ** 31 - 1, cin=65535 * 16, ldx=65535 * 16, ldy=2 ** 31, packed=Y0 + (1 << 36)), "overlaps"),
     (dict(x=Y0 + 32, ldx=80, ldy=40), None),  # x and y as columns of one buffer
     (dict(x=Y0 + 16, ldx=80, ldy=40), "y overlaps x"),
 ])
