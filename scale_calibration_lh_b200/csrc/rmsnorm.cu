@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(U == 1 ? 1024 : 512, K == 8 && U == 2 && sizeo
 // Rows of any length, read again for the output: from residual_out where there is one, since the
 // residual may have been updated in place.
 template <typename T, typename WT, int K>
-__global__ void __launch_bounds__(1024) rmsnorm_long_kernel(const RmsnormArgs a) {
+__global__ void __launch_bounds__(1024, sizeof(T) == 4 ? 2 : 1) rmsnorm_long_kernel(const RmsnormArgs a) {
   __shared__ float2 red[32];
   const Row<T> row(a, blockIdx.x);
   const int units = static_cast<int>(a.cin / K), span = blockDim.x, tid = threadIdx.x;
