@@ -311,6 +311,8 @@ lhcal_status lhcal_unpack_weights(const uint8_t* packed, const uint8_t* codes, c
  *   packed, codes, g : the packed weights [groups, rows, cin/2] (8-byte aligned; 16 is faster),
  *             their scale codes [groups, rows, cin/16] (E4M3 bit patterns in [0, 126], as every
  *             call here writes them; others give unspecified results) and global scales [groups].
+ *             Up to 15 bytes before codes and 8 before packed, in the 16-byte unit of their first byte,
+ *             may be read; they count for nothing.
  *   ytype, y: LHCAL_BF16 (rounded once from fp32) or LHCAL_F32 [slots, rows], row stride ldy
  *             elements (>= rows), aligned to its element size; overlapping no input
  *             (LHCAL_ERR_INVALID_ARG).

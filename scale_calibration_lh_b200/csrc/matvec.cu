@@ -23,10 +23,10 @@
 // split the channels, 256 to a warp and pass, and hold their activations while the rows go by;
 // their sums meet in shared memory in a fixed order, a block of rows at a time.
 //
-// Measured (us): 1 x 1280 x 2560 4.4, 1 x 4096 x 4096 5.9, 1 x 65536 x 4096 29.3 (5.2 TB/s), 1 x 467200 x 2560 114
-// (5.9 TB/s), 4 x 12288 x 4096 E4M3 9.5 (3.0 TB/s), routed 1 x 10 of 512 experts 1280 x 2560 10.4, 8 x 10
-// 32.5 (4.2 TB/s), 64 x 10 136 (5.0 TB/s). Bound by HBM where the rows are many; else by instructions (16
-// for 8 weights of a lane, 4 of them conversions; before the last step a tile took a warp 1450 cycles, of which 940 issued)
+// Measured (us): 1 x 1280 x 2560 4.3, 1 x 4096 x 4096 5.9, 1 x 65536 x 4096 29.3 (5.2 TB/s), 1 x 467200 x 2560 114
+// (5.9 TB/s), 4 x 12288 x 4096 E4M3 9.6 (3.0 TB/s), routed 1 x 10 of 512 experts 1280 x 2560 10.4, 8 x 10
+// 33 (4.2 TB/s), 64 x 10 136 (5.0 TB/s). Bound by HBM where the rows are many; else by instructions (16
+// for 8 weights of a lane, 20 where an entry has more than two slots, 4 of them conversions; before the last step a tile took a warp 1450 cycles, of which 940 issued)
 // and by what comes first: 1200 cycles until the shares are known (routed 3000), 2000 to 3000 for the
 // activations, while the ring fills. All loads of a tile go before its products (1 x 467200 x 2560: 121 ->
 // 114, 4 x 12288 x 4096 10.1 -> 9.5).

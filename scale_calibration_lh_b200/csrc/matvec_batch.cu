@@ -14,8 +14,8 @@
 // of its own (cp.async), a block ahead. Sums meet at a tile's end in a fixed order: the warpgroups'
 // through tensor memory, the cluster's through its shared memory.
 //
-// Measured (us): 17 x 4096 x 12288 E4M3 17.4, 16 x 4096 x 4096 8.4, 32 x 12288 x 4096 22, 64 x 4096 x 4096
-// 16.5, 64 x 12288 x 4096 32 (22, 11.0, 29.5, 27.5 and 64 with m16n8k16 products and each weight decoded
+// Measured (us): 17 x 4096 x 12288 E4M3 17.5, 16 x 4096 x 4096 8.5, 32 x 12288 x 4096 22, 64 x 4096 x 4096
+// 16.1, 64 x 12288 x 4096 32 (22, 11.0, 29.5, 27.5 and 64 with m16n8k16 products and each weight decoded
 // once a warp). Bound by latency: 64 x 12288 x 4096 takes 64 000 cycles with 48% of the issue slots used,
 // 12 000 of them until the first activations are there and converted, 24 blocks of 128 channels at 1250,
 // and 6 000 to join a tile's sums. Two operands of 64 channels a warpgroup, the next decoded while the

@@ -12,10 +12,10 @@
 // is read and written once; rows of more than 16384 channels (fp32: 8192) are read again. CTAs are small,
 // so that the SM always has rows that load, rows that reduce and rows that store.
 //
-// Measured: 16384 x 4096 bf16 with residual to E4M3 per 128 channels 72.6 us (6.5 TB/s), bf16 to bf16 82 us
-// (6.6 TB/s), fp32 8192 x 4096 68 us (6.4 TB/s), 1037 x 2560 bf16 4.6 us, one row of 4096 2.6 us: HBM, and
+// Measured: 16384 x 4096 bf16 with residual to E4M3 per 128 channels 73.8 us (6.4 TB/s), bf16 to bf16 83 us
+// (6.5 TB/s), fp32 8192 x 4096 70 us (6.2 TB/s), 1037 x 2560 bf16 4.6 us, one row of 4096 2.7 us: HBM, and
 // for few rows the latency of a load, a reduction and a store. Without a residual the 8-bit output is
-// bound by instructions (16384 x 2560: 34 us, 3.7 TB/s).
+// bound by instructions (16384 x 2560: 36 us, 3.5 TB/s).
 #include <cuda_fp8.h>
 
 #include <cfloat>
@@ -401,7 +401,8 @@ void launch_rows(const RmsnormArgs& a, cudaStream_t stream) {
                    dim3(threads, rows), args, 0, stream);
 }
 
-// How a row is shared out (bf16, us; 8 x 1: a unit of 8 channels a thread):
+// How a row is shared out (bf16, us; 8 x 1: a unit of 8 channels a thread; measured before the quotients were
+// corrected by their remainders, which adds 1 to 4% to each form with an 8-bit output):
 //   one 16-byte load a thread where the SMs then hold all rows at once, and for rows of one warp:
 //     600 x 1024 8 x 1 3.1, 8 x 2 3.5, 16 x 2 3.9; 60000 x 256 22.3, 24.6, 32.7;
 //   else, with an 8-bit output, fewer and longer units, for fewer maxima to be joined and quotients:
